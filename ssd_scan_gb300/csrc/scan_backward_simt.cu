@@ -647,11 +647,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) scan_bwd_simt_kerne
     }
 }
 
+// The local kernel's limit, the same for every shape (the largest takes 78,848 bytes): a
+// limit set to a call's own need would be lowered under the launch of another thread.
+constexpr size_t kLocalSmem = 96 * 1024;
+
 template <typename T> cudaError_t launch_local(const ScanBwdParams& p, int Q, cudaStream_t st)
 {
     const size_t smem = sizeof(float) * (size_t)Q * (row_stride(p.N) + local_stride(p.P));
     auto kern = scan_bwd_local_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> done[kMaxDevices];
+    const cudaError_t e = allow_smem((const void*)kern, kLocalSmem, done);
     if (e != cudaSuccess) return e;
     const long long blocks = 2LL * p.B * (((long long)p.S + Q - 1) / Q) * p.H;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;

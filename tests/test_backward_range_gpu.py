@@ -2,10 +2,13 @@
 
 Tolerances as derived in tests/test_backward_gpu.py.
 """
+import ctypes
+import threading
+
 import pytest
 import torch
 
-from tests.test_backward_gpu import BF16, TOL_F32_TC, TOL_TC, _check, _scan_got, _scan_problem, _scan_want
+from tests.test_backward_gpu import BF16, F32, TOL_F32_TC, TOL_TC, _check, _scan_got, _scan_problem, _scan_want
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +48,38 @@ def test_large_finite_rows_give_finite_gradients(S, log2):
     _check(got.dxbc[..., x:], want["dxbc"][..., x:], TOL_TC, "dB | dC")
     for n in ("ddt", "dA", "dD", "dssm_state"):
         _check(getattr(got, n), want[n], TOL_F32_TC, n)
+
+
+def test_threads_with_shapes_of_their_own():
+    """Calls from several threads, whose kernels need different amounts of
+    shared memory: each gets what it gets alone.  The C calls alone, so that
+    they meet; 4 threads whose first kernel needs 75 or 50 KB, 4 with 13 KB."""
+    lib = ssd.load_library()
+    shapes = 2 * [(1, 4, 1, 480, 64, 1), (1, 4, 2, 16, 16, 1), (1, 4, 1, 128, 256, 1), (1, 4, 1, 32, 16, 1)]
+    jobs = []
+    for k, (B, S, H, P, N, G) in enumerate(shapes):
+        t = _scan_problem(B, S, H, P, N, G, F32, seed=30 + k)
+        want = _scan_got(t, H, P, N, G)
+        out = ssd.ScanGrads(*(torch.empty_like(v) for v in want))
+        d = ssd.dims(B, S, H, P, N, G)
+        ws = torch.empty(ssd.ssd_chunk_scan_backward_workspace_size(d, ssd.SSD_F32), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        ptrs = [t[n].data_ptr() for n in ("xbc", "dt", "dt_bias", "A", "D", "h0", "dy", "dhS")] + [v.data_ptr() for v in out]
+        args = [ctypes.byref(d), ssd.SSD_F32, ssd.SSD_DT_SOFTPLUS, *ptrs, ws.data_ptr(), ws.numel(), stream.cuda_stream]
+        jobs.append((args, t, ws, stream, out, want))
+    torch.cuda.synchronize()
+    status = [set() for _ in jobs]
+
+    def work(k):
+        for _ in range(3000):
+            status[k].add(lib.ssd_chunk_scan_backward(*jobs[k][0]))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(jobs))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert all(st == {ssd.SSD_OK} for st in status), status
+    for *_, out, want in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
