@@ -20,7 +20,8 @@ constexpr int kMaxRows = 32;
 __global__ void __launch_bounds__(32 * kMaxRows) grad_reduce_kernel(GradReduceParams p)
 {
     __shared__ float part[kMaxRows][32];
-    sm100::griddep_wait();  // the partial sums
+    // the partial sums; plain loads, as they were not there when this grid began
+    sm100::griddep_wait();
     const int k = blockIdx.y;
     float* out = p.out[k];
     if (out == nullptr) return;
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(32 * kMaxRows) grad_reduce_kernel(GradReducePa
         for (int i = rg; i < p.nblk; i += 4 * rows)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (i + j * rows < p.nblk) acc[j] += __ldg(src + (size_t)(i + j * rows) * step);
+                if (i + j * rows < p.nblk) acc[j] += src[(size_t)(i + j * rows) * step];
     }
     part[rg][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
     __syncthreads();

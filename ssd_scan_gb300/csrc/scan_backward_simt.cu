@@ -113,7 +113,9 @@ __device__ __forceinline__ float2 lo2(float4 v) { return make_float2(v.x, v.y); 
 __device__ __forceinline__ float2 hi2(float4 v) { return make_float2(v.z, v.w); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+// (fp32: the boundary states too, which the kernel before writes while this one is
+// already there, so no read-only load)
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p)
 {
     const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
@@ -696,7 +698,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const float* part, T* dxbc, long long rows, int lead, int cols, int split)
 {
     sm100::griddep_launch_dependents();
-    sm100::griddep_wait();  // the shares
+    sm100::griddep_wait();  // the shares (plain loads: they were not there when this grid began)
     const int nv = cols / V, per = max(1, 256 / nv);
     const int r = threadIdx.x / nv;
     const long long row = (long long)blockIdx.x * per + r;
@@ -707,10 +709,10 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const float* part, T
 #pragma unroll 4
         for (int m = 0; m < split; ++m, src += rows * cols) {
             if (V == 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+                const float4 v = ld4(src);
                 acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
             } else {
-                acc[0] += __ldg(src);
+                acc[0] += *src;
             }
         }
         T* dst = dxbc + row * ((long long)lead + cols) + lead + k;

@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
         uint8_t* out = reinterpret_cast<uint8_t*>(back ? p.lout : p.hin) + unit * (2 * kStateBytes) +
                        (p0 >> 3) * kStatePitch + n * 16;
         float st[32];
+        // (plain loads: dh0 may be the same memory, written by this thread at the end)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) st[k] = init ? __ldg(init + sb + (size_t)(p0 + k) * N + n) : 0.0f;
+        for (int k = 0; k < 32; ++k) st[k] = init ? init[sb + (size_t)(p0 + k) * N + n] : 0.0f;
         const float* vals = p.vals + unit * kValStride;
         griddep_wait();  // the row values
         // the row's factor, and the chunk's decay
