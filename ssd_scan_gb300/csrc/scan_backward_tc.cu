@@ -899,7 +899,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 2; ++k) s.rho[k][0][row] = s.sig[k][0][row] = s.gx[k][warp] = 0.0f;  // no share of its own
         if (lane == 0) mbar_arrive(&s.cbread);
         ok = ctl_run();
-        if (!ok) set_abort(s);
+        if (!ok) {
+            set_abort(s);
+            // the walk may still run, and writes to the call's scratch and outputs: a CTA
+            // that gave up early must not let the stream go on before it
+            griddep_wait();
+        }
 #pragma unroll
         for (int k = 0; k < 16; ++k) facc[k] = make_float2(0.0f, 0.0f);
     } else {

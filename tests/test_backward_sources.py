@@ -3,7 +3,9 @@ their sources (CPU).
 
 A kernel launched while the one before it ends must load what that one wrote
 with ordinary loads, behind its wait: __ldg asks for memory that nobody writes
-while the kernel runs, and may be moved above the wait.
+while the kernel runs, and may be moved above the wait.  It also waits on every
+way out: what follows it on the stream starts when it is done, not when the one
+before it is.
 """
 import os
 import re
@@ -48,3 +50,23 @@ def test_overlapped_kernels_use_no_read_only_loads():
     code = _code("scan_backward_simt.cu")
     for m in re.finditer(r"float4 (?:load4|ld4)\(const float\*", code):
         assert "__ldg" not in _block(code, m.end())
+
+
+def test_overlapped_kernels_wait_on_every_way_out():
+    for name, kernel, body in _kernels():
+        if "griddep_wait()" not in body:
+            continue
+        wait = body.index("griddep_wait()")
+        if not re.search(r"\breturn\b", body[:wait]) and not re.search(r"\bif\b", body[:wait]):
+            continue  # before anything else
+        if kernel == "scan_bwd_tc_kernel":
+            # the control warp's run over the heads waits before it reads the states;
+            # one that ends before that does so after it
+            fail = body.index("if (!ok)", body.index("ok = ctl_run();"))
+            assert "griddep_wait()" in _block(body, fail)
+        elif kernel == "scan_bwd_states_tc_kernel":
+            # every warp that walks, before it waits for anything else
+            walk = _block(body, body.index("else", body.index("drain(&s.full")))
+            assert "griddep_wait()" in walk and "warp_wait" not in walk[:walk.index("griddep_wait()")]
+        else:
+            assert not re.search(r"\breturn\b", body[:wait]), (name, kernel)
