@@ -681,13 +681,13 @@ template <typename T> cudaError_t launch_chunks(const ScanBwdParams& p, cudaStre
 {
     ChunkShape c;
     if (!chunk_shape(p.P, p.N, &c)) return cudaErrorInvalidValue;
+    // N is a power of two up to 512, as the forward's; chunks have 16 rows only for head
+    // sizes from 493 on, which go with N up to 64
     switch (c.Q + (p.N + 127) / 128) {
         case 33: return launch_chunks_t<T, 4, 1>(p, c, st);
         case 34: return launch_chunks_t<T, 4, 2>(p, c, st);
-        case 35: return launch_chunks_t<T, 4, 3>(p, c, st);
+        case 36: return launch_chunks_t<T, 4, 4>(p, c, st);
         case 17: return launch_chunks_t<T, 2, 1>(p, c, st);
-        case 18: return launch_chunks_t<T, 2, 2>(p, c, st);
-        case 19: return launch_chunks_t<T, 2, 3>(p, c, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -748,7 +748,7 @@ int scan_bwd_simt_slots(int P, int N)
 int scan_bwd_simt_chunk(int P, int N)
 {
     ChunkShape c;
-    return scan_simt_supports(P, N) && N <= 384 && chunk_shape(P, N, &c) ? c.Q : 0;
+    return scan_simt_supports(P, N) && chunk_shape(P, N, &c) ? c.Q : 0;
 }
 
 cudaError_t launch_scan_bwd_local(const ScanBwdParams& p, bool bf16, cudaStream_t st)

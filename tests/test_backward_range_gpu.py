@@ -8,7 +8,7 @@ import threading
 import pytest
 import torch
 
-from tests.test_backward_gpu import BF16, F32, TOL_F32_TC, TOL_TC, _check, _scan_got, _scan_problem, _scan_want
+from tests.test_backward_gpu import BF16, F32, TOL_F32_TC, TOL_TC, _check, _scan_check, _scan_got, _scan_problem, _scan_want
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,25 @@ def test_threads_with_shapes_of_their_own():
     assert all(st == {ssd.SSD_OK} for st in status), status
     for *_, out, want in jobs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("act", [F32, BF16])
+@pytest.mark.parametrize("S,H,P,G", [(1, 2, 64, 1), (45, 4, 64, 2), (70, 3, 16, 1), (33, 2, 4, 2)])
+def test_scan_gradients_of_states_of_512(S, H, P, G, act):
+    """The widest state that the forward takes, as it takes it."""
+    N = 512
+    t = _scan_problem(2, S, H, P, N, G, act, seed=40)
+    ssd.chunk_scan(t["xbc"], t["dt"], t["A"], nheads=H, headdim=P, dstate=N, ngroups=G)
+    _scan_check(_scan_got(t, H, P, N, G), _scan_want(t, H, P, N, G), act, False)
+
+
+@pytest.mark.parametrize("act", [F32, BF16])
+@pytest.mark.parametrize("S,H,P,N,G", [(37, 1, 512, 32, 1), (16, 2, 1024, 16, 2), (50, 3, 500, 64, 1), (50, 2, 500, 64, 1), (1, 1, 640, 8, 1)])
+def test_scan_gradients_of_wide_heads(S, H, P, N, G, act):
+    """Head sizes whose chunks have 16 rows, the last one partly filled; a head
+    size that is not a multiple of the columns a warp takes."""
+    if act == BF16 and (H * P + 2 * G * N) % 8:
+        pytest.skip("rows of whole 16-byte vectors")
+    t = _scan_problem(2, S, H, P, N, G, act, seed=41)
+    ssd.chunk_scan(t["xbc"], t["dt"], t["A"], nheads=H, headdim=P, dstate=N, ngroups=G)
+    _scan_check(_scan_got(t, H, P, N, G), _scan_want(t, H, P, N, G), act, False)
