@@ -105,3 +105,16 @@ def test_scan_gradients_of_wide_heads(S, H, P, N, G, act):
     t = _scan_problem(2, S, H, P, N, G, act, seed=41)
     ssd.chunk_scan(t["xbc"], t["dt"], t["A"], nheads=H, headdim=P, dstate=N, ngroups=G)
     _scan_check(_scan_got(t, H, P, N, G), _scan_want(t, H, P, N, G), act, False)
+
+
+@pytest.mark.parametrize("B,S,H,G", [(40, 32, 8, 2), (500, 3, 8, 1), (17, 2, 32, 8), (100, 20, 24, 3)])
+def test_large_batches_of_short_sequences_on_the_tensor_cores(B, S, H, G):
+    """Few rows a sequence, many in all; the fp32 pipes keep calls of up to 32 rows."""
+    P, N = 64, 128
+    before = ssd.ssd_launch_counts()
+    t = _scan_problem(B, S, H, P, N, G, BF16, seed=90 + S)
+    _scan_check(_scan_got(t, H, P, N, G), _scan_want(t, H, P, N, G), BF16, True)
+    few = _scan_problem(32 // S, S, H, P, N, G, BF16, seed=91)
+    _scan_check(_scan_got(few, H, P, N, G), _scan_want(few, H, P, N, G), BF16, False)
+    after = ssd.ssd_launch_counts()
+    assert [after[k] - before[k] for k in ("scan_backward_tc", "scan_backward_simt")] == [1, 1]
