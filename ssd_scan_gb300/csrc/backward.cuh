@@ -7,8 +7,6 @@
 
 #include <cuda.h>
 
-#include <atomic>
-
 namespace ssd {
 
 // ---- host side ----------------------------------------------------------------
@@ -16,22 +14,6 @@ namespace ssd {
 // box_cols x box_rows, with the 128-byte swizzle or none.
 bool make_rows_map(CUtensorMap* m, const void* base, int elem, long long cols, long long rows, int batches,
                    int box_cols, int box_rows, bool swizzle);
-
-// A kernel's shared-memory limit, raised once per device.
-constexpr int kMaxDevices = 64;
-inline cudaError_t allow_smem(const void* fn, size_t bytes, std::atomic<bool> (&done)[kMaxDevices])
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    // (not left to the driver, which may keep room for L1 and lose a resident CTA)
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
-    return e;
-}
 
 // Launched to overlap the end of the kernel before it on the stream, which is
 // one of this call's: the kernel waits for it before it reads its results.

@@ -230,8 +230,8 @@ template <typename T, int KT, int RF, bool kZs>
 cudaError_t launch_kz(const DecodeParams& p, cudaStream_t st)
 {
     const size_t smem = decode_smem_bytes(p.H, p.P, p.N, p.G, p.K, kZs);
-    cudaError_t e = cudaFuncSetAttribute(decode_step_kernel<T, KT, RF, kZs>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> done[kMaxDevices];
+    const cudaError_t e = allow_smem((const void*)decode_step_kernel<T, KT, RF, kZs>, kDecodeSmemMax, done, false);
     if (e != cudaSuccess) return e;
     decode_step_kernel<T, KT, RF, kZs><<<dim3(p.G, p.R), kThreads, smem, st>>>(p);
     return cudaGetLastError();

@@ -6,7 +6,27 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace ssd {
+
+// A kernel's dynamic shared-memory limit, raised once per device to the most that
+// any call needs (set to each call's own need, a call of another thread could lower
+// it before the launch).  most_for_smem: the SM's memory divided for it as well, not
+// left to the driver, which may keep room for L1 and lose a resident CTA.
+constexpr int kMaxDevices = 64;
+inline cudaError_t allow_smem(const void* fn, size_t bytes, std::atomic<bool> (&done)[kMaxDevices], bool most_for_smem = true)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && most_for_smem)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // Bits of the per-device error word (first error kind wins in the report).
 enum : unsigned { kErrBadSlot = 1u, kErrTimeout = 2u, kErrDupSlot = 4u };

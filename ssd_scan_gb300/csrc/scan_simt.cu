@@ -168,8 +168,8 @@ cudaError_t launch_t(const ScanParams& p, const SimtShape& s, cudaStream_t st)
                                          (size_t)HW * CH + 2 * kRows +
                                          (p.conv_w ? (size_t)CH * (p.W + 1) : 0));
     auto kern = scan_simt_kernel<T, NPT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    static std::atomic<bool> done[kMaxDevices];
+    const cudaError_t e = allow_smem((const void*)kern, 227 * 1024, done, false);
     if (e != cudaSuccess) return e;
     dim3 grid(p.H, p.B);
     kern<<<grid, s.threads, smem, st>>>(p, s.nq);
