@@ -104,7 +104,8 @@ __device__ __forceinline__ void sums(const float2* y, const float2* z, const flo
         sd = __ffma2_rn(__fmul2_rn(__fmul2_rn(d[i], __fmul2_rn(z[i], q[i])), w[i]), y[i], sd);
     }
 }
-// its gradients; m = r^2 sum(dn y) / gs, to be multiplied by y
+// its gradients; m = r^2 sum(dn y) / gs, to be multiplied by y (r times r sum(dn y)
+// / gs, which is of dn's size: r^2 alone overflows for rows below 2^-64)
 template <int V>
 __device__ __forceinline__ void grads(const float2* y, const float2* z, const float2* d, const float2* w, const float2* q, float r,
                                       float m, float2* oy, float2* oz, float2* dw)
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32) gated_norm_bwd_kernel(GatedNormBw
             sums<V>(y, z, d, wv, q[k], s2, d2);
         }
         const float ss = warp_sum(s2.x + s2.y), sd = warp_sum(d2.x + d2.y);
-        const float r = rsqrtf(ss * inv + p.eps), m = r * r * sd * inv;
+        const float r = rsqrtf(ss * inv + p.eps), m = r * (r * (sd * inv));
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int e = (k * 32 + lane) * V;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 256 ? 3 : 1) gated
             ss += part[par][0][i];
             sd += part[par][1][i];
         }
-        const float r = rsqrtf(ss * inv + p.eps), m = r * r * sd * inv;
+        const float r = rsqrtf(ss * inv + p.eps), m = r * (r * (sd * inv));
         float2 oy[H], oz[H];
         grads<V>(y, z, d, w, q, r, m, oy, oz, dw);
         if (in) {
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kWide) gated_norm_bwd_wide_kernel(GatedNormBwd
             ss += part[par][0][i];
             sd += part[par][1][i];
         }
-        const float r = rsqrtf(ss * inv + p.eps), m = r * r * sd * inv;
+        const float r = rsqrtf(ss * inv + p.eps), m = r * (r * (sd * inv));
         for (int e = tid * V; e < gs; e += kWide * V) {
             load(e);
             float2 oy[H], oz[H], sum[H];
