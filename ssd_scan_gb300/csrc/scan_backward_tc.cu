@@ -112,6 +112,16 @@ __device__ __forceinline__ void df_to_log2(float hi, float lo, float& rh, float&
     rl = e - (rh - p);
 }
 
+// 2^min(a - b, most) of double-floats: with the difference in fp32 alone the result
+// would be off by half a step of it, 2e-6 of 2^60
+__device__ __forceinline__ float exp2_diff(float ah, float al, float bh, float bl, float most)
+{
+    const float s = ah - bh, v = s - ah;
+    const float e = ((ah - (s - v)) - (bh + v)) + (al - bl);  // what s left out
+    const float t = s + e, r = e - (t - s);
+    return t < most ? ex2_fast(t) * fmaf(r, 0.6931471806f, 1.0f) : ex2_fast(most);
+}
+
 __device__ __forceinline__ uint32_t pack2(float2 a)
 {
     __nv_bfloat162 h = __float22bfloat162_rn(a);
@@ -248,8 +258,8 @@ __global__ void __launch_bounds__(32 * kRowHeads) scan_bwd_rows_kernel(ScanBwdTc
         float w[4], u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = exp2f(fminf((qh - oh[i]) + (ql - ol[i]), 0.0f));
-            u[i] = exp2f(fminf(oh[i] + ol[i], 0.0f));
+            w[i] = exp2_diff(qh, ql, oh[i], ol[i], 0.0f);
+            u[i] = exp2_diff(oh[i], ol[i], 0.0f, 0.0f, 0.0f);
         }
         float4* out = reinterpret_cast<float4*>(p.vals + (((size_t)b * p.H + h) * nc + c) * kValStride);
         out[kDt * 32 + lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
@@ -266,11 +276,11 @@ __global__ void __launch_bounds__(32 * kRowHeads) scan_bwd_rows_kernel(ScanBwdTc
             if (!((fh - mh) + (fl - ml) <= kSplitMaxLog2)) exact |= 1 << k;
             float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = ex2_fast(fminf((oh[i] - mh) + (ol[i] - ml), kSplitMaxLog2));
+            for (int i = 0; i < 4; ++i) v[i] = exp2_diff(oh[i], ol[i], mh, ml, kSplitMaxLog2);
             if ((lane >> 3) >= k) out[(kUb + k) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
             if ((lane >> 3) == k) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = ex2_fast(fminf((mh - oh[i]) + (ml - ol[i]), 0.0f));
+                for (int i = 0; i < 4; ++i) v[i] = exp2_diff(mh, ml, oh[i], ol[i], 0.0f);
                 out[kV * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
