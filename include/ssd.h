@@ -440,10 +440,10 @@ SSD_API ssd_status ssd_conv1d_rows_backward_workspace_size(const ssd_dims* dims,
  *                   dssm_state_out exactly
  * flags: SSD_DT_SOFTPLUS; SSD_HAS_Z gives SSD_ERR_UNSUPPORTED (train with the
  * scan ungated and the gated norm behind it).  In bf16 with P = 64 and N = 128
- * the states carry 16 bits on the way to the tensor cores (calls of more than
+ * the states carry 17 bits on the way to the tensor cores (calls of more than
  * 6 heads, and of more than 32 heads or more than 32 rows in all sequences):
- * fp32 gradients are off by about 1e-6 of their size, dA and ddt_bias by more
- * where the terms of a head cancel.  dims->chunk as in
+ * fp32 gradients are off by 2e-7 to 7e-7 of their size, dA and ddt_bias by more
+ * where the terms of a head cancel (otherwise 1e-7 to 4e-7).  dims->chunk as in
  * ssd_chunk_scan; conv_width is not used.  Shapes as ssd_chunk_scan's, and at
  * most 65535 sequences, 2047 groups, and in bf16 with P = 64 and N = 128
  * 524280 heads and 2^30 chunks of 128 rows, otherwise 2^30 chunks of 16 or 32

@@ -36,22 +36,28 @@
 // columns) and its operands shared memory (225 KB).
 //
 // Measured, 128 heads in 8 groups (us, rows / states / chunks): one sequence of
-// 2048 rows 7 / 42 / 70, the call 118; 2 x 8192 rows 19 / 313 / 465, the call 800.
-// The states kernel moves 128 KB between L2 and its SM a step at 7 TB/s in all,
-// and is bound by that.  The chunk kernel is bound by the work around its
-// products: 4.4 us a head, of which the tensor pipe is busy 1.2; the masks issue on
-// every scheduler for a third of the time, the rest is the chain from one
-// product's end over TMEM to the next one's operands.
+// 2048 rows 8 / 45 / 71, the call 122; 2 x 8192 rows 25 / 339 / 468, the call 830.
+// The states kernel moves 128 KB between L2 and its SM a step, 6.4 TB/s in all,
+// and its steps (5,500 cycles) are the product of 24 (1,500), the way of its result over
+// TMEM to the next one's operands, and the scaling of rows between.  The chunk kernel is
+// bound by the work around its products: 4.4 us a head, of which the tensor pipe is busy
+// 1.2; the masks issue on every scheduler for a third of the time, the rest is the chain
+// from one product's end over TMEM to the next one's operands.
 //
 // Precision.  x, g, B and C are bf16 already.  ddt, dA, ddt_bias, dD and the
-// initial state's gradient are fp32: everything they depend on keeps at least
-// 16 bits, so the states (and the scaled rows that make them) are two bf16,
-// hi + lo, each product run on both.  K = E (g.x), whose sums da is made of,
-// never leaves fp32.  Only what ends in a bf16 output takes single bf16
-// operands: E, F, u o g and w dt o x.  (Against 64 bits: ddt off by 6e-7 of its
-// 2-norm, the initial state's gradient 2.5e-6, dA 1e-6 and more where a head's
-// terms cancel; a third bf16 would bring them to fp32 for half as much again of
-// the states' traffic.)
+// initial state's gradient are fp32.  The states are sums in fp32 registers of products
+// that see all 24 bits of the scaled rows (three bf16, one product on each, the
+// smallest first).  On their way to the chunks they are two bf16, hi + lo, 17 bits, in
+// the bytes of one fp32, and each product with them runs on both: off by 2^-17 of an
+// element at most.  K = E (g.x), whose sums da is made of, never leaves fp32.  Only what ends in
+// a bf16 output takes single bf16 operands: E, F, u o g, w dt o x and, beside these two,
+// the states.  Against 64 bits, in the 2-norm: ddt 4.5e-7, dA 4.6e-7 to 6e-7 and ddt_bias
+// 5e-7 to 7e-7, more where the terms of a head cancel, the initial state's gradient
+// 2.3e-7; all fp32 would be 1e-7 to 4e-7.  With two bf16 for the scaled rows as well ddt was
+// 7.5e-7, dA 1.1e-6 to 2e-6 and the initial state's gradient 2.5e-6, at 117 us for the
+// 2048 rows.  Three for the states on their way too, made from fp32 by the chunk kernel: 2.8e-7
+// and 3.0e-7, and 154 us, as the products with them already take all of shared memory's
+// bandwidth while they run.
 //
 // da_t sums the terms that cross row t, with no difference of large sums: in
 // 32-row blocks, whole blocks of K below and left of t, partial row sums and
@@ -139,7 +145,7 @@ __device__ __forceinline__ uint4 pack8(const float2* f)
 {
     return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
-// v = hi + lo in two bf16 each: off by at most 2^-16 of the value
+// v = hi + lo in two bf16 each: off by at most 2^-17 of the value
 __device__ __forceinline__ void split8(const float2* v, uint4& hi, uint4& lo)
 {
     float2 r[4], h[4];
@@ -150,6 +156,18 @@ __device__ __forceinline__ void split8(const float2* v, uint4& hi, uint4& lo)
     lo = pack8(r);
 }
 
+// v = hi + mid + lo in bf16 each, a pair of them: all of v's 24 bits.  hi is rounded (it
+// stands for v alone in some products); what it leaves has 16 bits, whose upper
+// and lower half are mid and lo.
+__device__ __forceinline__ uint32_t upper2(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo)
+{
+    hi = pack2(v);
+    const float2 h = unpack2(hi), r = make_float2(v.x - h.x, v.y - h.y);
+    mid = upper2(r);
+    const float2 m = unpack2(mid);
+    lo = upper2(make_float2(r.x - m.x, r.y - m.y));
+}
 // byte offset of 16-byte chunk j of row r in a SW128 tile of 64-element rows
 __device__ __forceinline__ uint32_t chunk_off(int r, int j) { return (uint32_t)(r * 128 + (((j ^ r) & 7) << 4)); }
 template <typename T> __device__ __forceinline__ T& at(void* base, uint32_t off)
@@ -302,15 +320,21 @@ constexpr int kStateBytes = N * P * 2;  // of one of the two
 // tiles, which halves that part of what the walk reads from L2, and one product
 // serves both (128 columns keep the tensor pipe twice as busy as 64).  While a
 // chunk's product runs, the value before it leaves and the next chunk's rows
-// are scaled: 42 us for 2048 rows of 128 heads, against 49 with the two in turn.
-constexpr int kStStages = 3;
+// are scaled: 45 us for 2048 rows of 128 heads (with two planes of the scaled rows 42,
+// and 49 with the two in turn).
+// So x and g, and mid of the scaled rows, have stages.  B or C has two as well where
+// there is room; otherwise it is asked for when the last product is done, some thousand
+// cycles before the rows of the next are ready.
+constexpr int kStX = 3;
 template <int kHeads> struct __align__(1024) StSmem {
-    __nv_bfloat16 M[kStStages][2][Q * 64];  // B or C tile [row][n], 2 panels of 64 n (TMA, SW128)
+    static constexpr int kM = kHeads == 1 ? 2 : 1;
+    __nv_bfloat16 M[kM][2][Q * 64];    // B or C tile [row][n], 2 panels of 64 n (TMA, SW128)
     struct {
-        __nv_bfloat16 X[kStStages][Q * 64]; // x or g tile [row][p]; scaled in place (hi)
-        __nv_bfloat16 L[Q * 64];            // the scaled rows' lo
+        __nv_bfloat16 X[kStX][Q * 64]; // x or g tile [row][p]; scaled in place (hi)
+        __nv_bfloat16 mid[2][Q * 64];  // the scaled rows' mid, by parity
+        __nv_bfloat16 lo[Q * 64];      // ... and lo
     } hd[kHeads];
-    uint64_t full[kStStages], ready, done;
+    uint64_t full_x[kStX], full_m[kM], ready, done;
     uint32_t tmem_base;
     int abort;
 };
@@ -323,7 +347,7 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
     scan_bwd_states_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                               const ScanBwdTcParams p)
 {
-    constexpr int kControl = 8 * kHeads;
+    constexpr int kControl = 8 * kHeads, kM = StSmem<kHeads>::kM;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     StSmem<kHeads>& s =
         *reinterpret_cast<StSmem<kHeads>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -339,7 +363,8 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
 
     if (warp == kControl) {
         if (lane == 0) {
-            for (int k = 0; k < kStStages; ++k) mbar_init(&s.full[k], 1);
+            for (int k = 0; k < kStX; ++k) mbar_init(&s.full_x[k], 1);
+            for (int k = 0; k < kM; ++k) mbar_init(&s.full_m[k], 1);
             mbar_init(&s.ready, 8 * kHeads);
             mbar_init(&s.done, 1);
             s.abort = 0;
@@ -358,49 +383,60 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
     if (warp == kControl) {
         const CUtensorMap* mx = back ? &map_g : &map_x;
         const int cm = H * P + (back ? G * N : 0) + g * N;
-        int nl = 0, nd = 0;  // loads and commits issued
-        auto load = [&]() {
+        int nx = 0, nm = 0, nd = 0;  // loads and commits issued
+        auto load_x = [&]() {
             if (elect_one()) {
-                const int k = nl % kStStages, r = chunk(nl) * Q;
-                uint64_t* bar = &s.full[k];
-                mbar_arrive_expect_tx(bar, (kHeads + 2) * Q * 64 * 2);
-                for (int m = 0; m < kHeads; ++m) tma_load_3d(s.hd[m].X[k], mx, bar, (h0 + m) * P, r, b);
-                tma_load_3d(s.M[k][0], &map_x, bar, cm, r, b);
-                tma_load_3d(s.M[k][1], &map_x, bar, cm + 64, r, b);
+                const int k = nx % kStX;
+                mbar_arrive_expect_tx(&s.full_x[k], kHeads * Q * 64 * 2);
+                for (int m = 0; m < kHeads; ++m) tma_load_3d(s.hd[m].X[k], mx, &s.full_x[k], (h0 + m) * P, chunk(nx) * Q, b);
             }
             __syncwarp();
-            ++nl;
+            ++nx;
         };
-        while (nl < min(steps, kStStages - 1)) load();
+        auto load_m = [&]() {
+            if (elect_one()) {
+                uint64_t* bar = &s.full_m[nm % kM];
+                mbar_arrive_expect_tx(bar, 2 * Q * 64 * 2);
+                tma_load_3d(s.M[nm % kM][0], &map_x, bar, cm, chunk(nm) * Q, b);
+                tma_load_3d(s.M[nm % kM][1], &map_x, bar, cm + 64, chunk(nm) * Q, b);
+            }
+            __syncwarp();
+            ++nm;
+        };
+        while (nx < min(steps, kStX - 1)) load_x();
+        while (nm < min(steps, kM)) load_m();
         bool ok = true;
         for (int i = 0; i < steps; ++i) {
-            const int k = i % kStStages;
             // the scaled rows; the last product has been taken out of TMEM by then, so
-            // its stage is free
-            if (!(ok = warp_wait(s, &s.ready, i & 1, wlim) && warp_wait(s, &s.full[k], (i / kStStages) & 1, wlim))) break;
+            // its stages are free
+            if (!(ok = warp_wait(s, &s.ready, i & 1, wlim) && warp_wait(s, &s.full_m[i % kM], (i / kM) & 1, wlim))) break;
             tc_fence_after();
-            const uint64_t dM = sdesc_sw128(smem_u32(s.M[k]), Q * 128, 1024);
+            const uint64_t dM = sdesc_sw128(smem_u32(s.M[i % kM]), Q * 128, 1024);
             const uint32_t lead = elect_one();
             // the heads side by side in one product: 64 columns each, a tile's
-            // distance apart
-            const uint64_t dX = sdesc_sw128(smem_u32(s.hd[0].X[k]), sizeof(s.hd[0]), 1024);
-            const uint64_t dL = sdesc_sw128(smem_u32(s.hd[0].L), sizeof(s.hd[0]), 1024);
+            // distance apart; the smallest plane first, as an addition cuts off bits of the sum
+            auto side = [&](const void* tile) { return sdesc_sw128(smem_u32(tile), sizeof(s.hd[0]), 1024); };
+            const uint64_t planes[3] = {side(s.hd[0].lo), side(s.hd[0].mid[i & 1]), side(s.hd[0].X[i % kStX])};
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-                mma_bf16_ss_by(lead, tb, dM + 128 * m, dX + 128 * m, idesc_state(kHeads), m > 0);
+            for (int q = 0; q < 3; ++q)
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-                mma_bf16_ss_by(lead, tb, dM + 128 * m, dL + 128 * m, idesc_state(kHeads), 1);
+                for (int m = 0; m < 8; ++m)
+                    mma_bf16_ss_by(lead, tb, dM + 128 * m, planes[q] + 128 * m, idesc_state(kHeads), q + m > 0);
             mma_commit_by(elect_one(), &s.done);
             ++nd;
-            if (nl < steps) load();
+            if (nx < steps) load_x();
+            if (nm < min(steps, i + 2)) {
+                if (kM == 1 && !(ok = warp_wait(s, &s.done, i & 1, wlim))) break;
+                load_m();
+            }
         }
         if (!ok) set_abort(s);
         if (elect_one()) {
             // nothing of ours in flight when the CTA leaves (bounded waits)
             const uint64_t t0 = globaltimer_ns();
             if (nd > 0) drain(&s.done, (nd - 1) & 1, t0);
-            for (int k = max(0, nl - kStStages); k < nl; ++k) drain(&s.full[k % kStStages], (k / kStStages) & 1, t0);
+            for (int k = max(0, nx - kStX); k < nx; ++k) drain(&s.full_x[k % kStX], (k / kStX) & 1, t0);
+            for (int k = max(0, nm - kM); k < nm; ++k) drain(&s.full_m[k % kM], (k / kM) & 1, t0);
         }
         __syncwarp();
     } else {
@@ -426,35 +462,43 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
             return back ? v[kU * Q + row] : v[kW * Q + row] * v[kDt * Q + row];
         };
         auto decay = [&](int i) { return vals[(size_t)chunk(i) * kValStride + kU * Q + Q - 1]; };  // exp(gamma_Q)
-        // rows of chunk i by their factor: hi in place, lo kept
+        // rows of chunk i by their factor: hi in place, mid to its stage, lo kept
         uint4 lo[4];
         auto scale = [&](int i, float f) -> bool {
-            const int k = i % kStStages;
-            if (!warp_wait(s, &s.full[k], (i / kStStages) & 1, wlim)) return false;
+            const int k = i % kStX;
+            if (!warp_wait(s, &s.full_x[k], (i / kStX) & 1, wlim)) return false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint4& x = at<uint4>(t.X[k], chunk_off(row, j0 + j));
-                float2 v2[4];
-                unpack8(x, v2);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) v2[m] = __fmul2_rn(v2[m], make_float2(f, f));
-                uint4 hi;
-                split8(v2, hi, lo[j]);
-                x = hi;
+                const uint32_t o = chunk_off(row, j0 + j);
+                const uint4 x = at<uint4>(t.X[k], o);
+                const float2 f2 = make_float2(f, f);
+                uint4 hi, mid;
+                split2(__fmul2_rn(unpack2(x.x), f2), hi.x, mid.x, lo[j].x);
+                split2(__fmul2_rn(unpack2(x.y), f2), hi.y, mid.y, lo[j].y);
+                split2(__fmul2_rn(unpack2(x.z), f2), hi.z, mid.z, lo[j].z);
+                split2(__fmul2_rn(unpack2(x.w), f2), hi.w, mid.w, lo[j].w);
+                at<uint4>(t.X[k], o) = hi;
+                at<uint4>(t.mid[i & 1], o) = mid;
             }
             return true;
         };
-        auto scaled = [&]() {
+        // lo, once no product reads the last one
+        auto put = [&]() {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) at<uint4>(t.L, chunk_off(row, j0 + j)) = lo[j];
+            for (int j = 0; j < 4; ++j) at<uint4>(t.lo, chunk_off(row, j0 + j)) = lo[j];
             fence_proxy_async_smem();
+        };
+        auto scaled = [&]() {
             tc_fence_before();  // the last step's TMEM loads
             warp_arrive(&s.ready, lane);
         };
         float fn = 0.0f, en = 0.0f;
         bool ok = true;
         if (steps > 0) {
-            if ((ok = scale(0, factor(0)))) scaled();
+            if ((ok = scale(0, factor(0)))) {
+                put();
+                scaled();
+            }
             en = decay(0);
             if (steps > 1) fn = factor(1);
         }
@@ -484,6 +528,7 @@ __global__ void __launch_bounds__(256 * kHeads + 32, 1)
             tc_fence_after();
             float d[32];
             tmem_ld32(taddr, d);
+            if (more) put();
             tmem_ld_wait();
             if (more) scaled();
 #pragma unroll
@@ -692,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lead = elect_one();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-            const uint64_t ak = a + 1024 * (k & 1), bk = (k < 2 ? hi : lo) + 64 * (k & 1);
+            const uint64_t ak = a + 1024 * (k & 1), bk = (k < 2 ? lo : hi) + 64 * (k & 1);
 #pragma unroll
             for (int m = 0; m < 4; ++m) mma_bf16_ss_by(lead, d, ak + 2 * m, bk + 16 * m, kIdQP, k + m > 0);
         }

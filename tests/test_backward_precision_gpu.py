@@ -1,6 +1,13 @@
 """How exact the tensor-core gradients' fp32 outputs are, in the 2-norm against
 64 bits, beyond the tolerances of tests/test_backward_gpu.py.
 
+The initial state's gradient: the walk over the chunks multiplies all 24 bits
+of the scaled rows, so a term carries the exponential (2^-22), the factor and
+the product (2^-24 each), and its way into the sum: 8 steps of the tensor
+pipe at the sum's size, which cut off up to 2^-23 each, and a rounding a chunk.
+In quadrature 2^-22 sqrt(1 + 8 / 4) and the roundings: under 2^-21 = 4.8e-7,
+twice that allowed.
+
 Gradients inside a chunk: the decay between two rows is the product of two
 exponentials (2^-22 each) of double-float differences, x . dy and C . B are sums
 of the tensor pipe (4 and 8 steps, 2^-23), and the sums over rows in fp32 trees
@@ -30,6 +37,14 @@ def _cuda():
 
 def _off(got, want):
     return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("B,S,H,G", [(1, 128, 8, 2), (2, 300, 8, 1), (2, 1111, 16, 1), (1, 700, 128, 8)])
+def test_initial_state_gradient(B, S, H, G):
+    t = _scan_problem(B, S, H, P, N, G, BF16, seed=100 + S)
+    t["dhS"] *= 0.0  # all of it from the rows
+    got, want = _scan_got(t, H, P, N, G), _scan_want(t, H, P, N, G)
+    assert _off(got.dssm_state, want["dssm_state"]) <= 2 * 2.0 ** -21
 
 
 @pytest.mark.parametrize("decay", [0.02, 0.3, 1.1])
