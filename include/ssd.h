@@ -426,6 +426,9 @@ SSD_API ssd_status ssd_conv1d_rows_backward_workspace_size(const ssd_dims* dims,
  *   dA = sum dt_t da_t,  dD = sum g_t . x_t,  ddt_bias = sum ddt_t (zeros
  *   without SSD_DT_SOFTPLUS, where dt_bias is ignored)
  *   dssm_state_in = exp(a_1) lam_1
+ * A row with dt_t A > 0 lies outside the conventions above (A negative, decay at
+ * most 1), and the forward's kernels treat it each in their own way; here it
+ * counts as decay 1, which no gradient passes.
  * The states are recomputed from ssm_state_in: nothing of the forward is kept
  * but its inputs.
  *

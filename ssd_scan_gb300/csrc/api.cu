@@ -581,16 +581,17 @@ struct ScanBwdSizes {
 };
 bool scan_bwd_sizes(const ssd_dims* d, ssd_dtype act, ScanBwdSizes* z)
 {
-    // Tensor cores / fp32 pipes: 2048 rows of 128 heads 116 / 1577 us, 100 rows of 8
-    // heads 21 / 40, 500 sequences of 32 rows of 32 heads 1006 / 4686.  Very few heads, or
-    // a few rows in all of a few heads, take the fp32 pipes although they are slower (32
-    // rows of 8 heads 18 / 48 us, 4 x 1965 rows of 5 heads 60 / 283): their dA, one
-    // number a head, can hang on one head whose terms cancel, and of such a head the 16
-    // bits of the tensor cores' states keep less.  The 2-norm over the heads was off by 2.5e-5
-    // / 2e-7 in the worst of a hundred calls for 2 rows of 5 heads, 1.9e-5 / 2e-7 for 4 x
-    // 1965 rows; with 7 to 24 heads and 33 to 512 rows in sequences of 2 to 32, 8.5e-6 / 1.3e-6
-    // in the worst of 480.  (Rows count over the batch: by their number in a sequence,
-    // large batches of short ones took four times as long.)
+    // Tensor cores / fp32 pipes, us on the GPU: 2048 rows of 128 heads 121 / 1450, 100 rows
+    // of 8 heads 22 / 37, 500 sequences of 32 rows of 32 heads 1018 / 4549.  Very few heads,
+    // or a few rows in all of a few heads, take the fp32 pipes although they are slower (32
+    // rows of 8 heads 18 / 37, 4 x 1965 rows of 5 heads 66 / 275): dA and ddt_bias are one
+    // number a head, in which the terms can cancel, and of such a head the 17 bits of the
+    // tensor cores' states leave less.  Off in the 2-norm over the heads, the worst of 150
+    // calls of 33 to 2800 rows: 1 head 1e-3 / 1e-4, 2 heads 5.4e-5 / 5.5e-6, 5 heads 1.4e-5 /
+    // 1.7e-6, 6 heads 1.1e-5 / 1.1e-6, 7 heads 4.9e-6; of 100 calls of 2 rows and more of 5
+    // heads 1.3e-5.  A head among many loses as much (the worst dA of 128: 1.4e-4); only the
+    // others' norm hides it.  (Rows count over the batch: counted a sequence, large batches of
+    // short ones took four times as long.)
     const long long rows = (long long)d->batch * d->seqlen;
     const bool few = d->nheads <= 6 || (rows <= 32 && d->nheads <= 32);
     z->tc = act == SSD_BF16 && d->seqlen > 0 && !few && scan_bwd_tc_supports(d->headdim, d->dstate);

@@ -18,8 +18,13 @@
 //
 // Measured, 10,240 channels of 4 taps, bf16: 2 x 8192 rows 205 us (4.9 TB/s of the
 // x, dout and dx bytes), 2048 rows 37 us with 4 of the final reduction.  With
-// loads to registers, a batch ahead, they took 344 and 53.  The packed multiply-adds
-// (19 a row and pair of channels) are the next bound, at some 21 us of 32.
+// loads to registers, a batch ahead, they took 344 and 53.  No one thing bounds the 32
+// us that the kernel takes of the 2048 rows: it issues 2.05 instructions a cycle of 4, of
+// the cycles between a warp's instructions 2.2 wait for its tiles and 1.9 for the fp32
+// pipe (19 packed multiply-adds a row and pair of channels), and DRAM is at 37 %.
+// A CTA's rows are one sequence's, so sequences shorter than its 256 rows (fp32: 128)
+// leave warps without work and add partial sums: 16,384 rows as 64 sequences take 201 us
+// on the GPU, as 256 426, as 512 735, as 2048 3204.
 #include "backward.cuh"
 #include "sm100.cuh"
 

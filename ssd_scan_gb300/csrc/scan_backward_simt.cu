@@ -27,8 +27,8 @@
 // its operands in shared memory.  Few chunks and groups: the heads of a group
 // are split over CTAs, whose shares of dB and dC are added afterwards.  Measured, 2 x
 // 500 rows of 8 heads in 2 groups, P = 64, N = 128, fp32: local 14 us, carry 10,
-// chunks 40, sums 8; the call, whose launches overlap, 61 us.  The chunk kernel's 1142 shared loads a warp
-// are 41,000 passes an SM of its 75,000 cycles, its multiply-adds 16,000.
+// chunks 40, sums 8; the call, whose launches overlap, 61 us.  The chunk kernel's shared-memory
+// accesses are 44,000 passes an SM of its 75,000 cycles, its multiply-adds 16,000.
 #include "backward.cuh"
 #include "sm100.cuh"
 

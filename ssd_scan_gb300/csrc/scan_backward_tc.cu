@@ -36,7 +36,7 @@
 // columns) and its operands shared memory (225 KB).
 //
 // Measured, 128 heads in 8 groups (us, rows / states / chunks): one sequence of
-// 2048 rows 8 / 45 / 71, the call 122; 2 x 8192 rows 25 / 339 / 468, the call 830.
+// 2048 rows 8 / 45 / 71, the call 121; 2 x 8192 rows 25 / 339 / 468, the call 830.
 // The states kernel moves 128 KB between L2 and its SM a step, 6.4 TB/s in all,
 // and its steps (5,500 cycles) are the product of 24 (1,500), the way of its result over
 // TMEM to the next one's operands, and the scaling of rows between.  The chunk kernel is
@@ -1296,8 +1296,8 @@ template <int kHeads> cudaError_t launch_states_t(const ScanBwdTcParams& p, TcMa
 cudaError_t launch_states(const ScanBwdTcParams& p, TcMaps& m, cudaStream_t st)
 {
     // two heads a CTA where that leaves a CTA for nearly every SM (the whole call: 2048
-    // rows of 128 heads 116 us, one head a CTA 126; 4 x 1111 rows of 16 heads 57, one
-    // head 50)
+    // rows of 128 heads 121 us, one head a CTA 137; 4 x 1111 rows of 16 heads 59, one
+    // head 53)
     const bool two = (p.H / p.G) % 2 == 0 && (long long)p.B * p.H >= 128;
     return two ? launch_states_t<2>(p, m, st) : launch_states_t<1>(p, m, st);
 }
