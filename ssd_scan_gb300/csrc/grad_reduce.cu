@@ -5,7 +5,7 @@
 // One CTA per 32 columns and part k: rows of threads walk the blocks (128
 // contiguous bytes per warp and block, about four blocks a thread), then meet in
 // shared memory.  Launched while the kernel before it ends; 3 to 10 us, mostly
-// latency (152 blocks of 8192 columns: 6 us for 5 MB).  No atomics: the order of the additions is fixed, so a gradient
+// latency (95 blocks of 8192 columns: 5 us for 3 MB).  No atomics: the order of the additions is fixed, so a gradient
 // has the same bits on every run.  In fp32, as a tree: at most ~8 roundings on
 // the way to a sum of a hundred terms (fp64 adds and conversions run at 1/64 of
 // the rate here and took most of the kernel's time).

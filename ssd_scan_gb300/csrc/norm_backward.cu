@@ -8,7 +8,7 @@
 // Both group means come out of one pass: sum y^2 and sum dn y (mean(dn n) =
 // r sum(dn y) / gs), so y, z and dout are read once and dy, dz written once.
 // HBM-bound: 5 C elements a row.  Measured, 8192 channels in 8 groups, bf16: 2 x
-// 8192 rows 249 us (5.4 TB/s), 2048 rows 40 us, 6 of them the final reduction.
+// 8192 rows 248 us (5.4 TB/s), 2048 rows 39 us, 5 of them the final reduction.
 //
 // Groups of up to 64 vectors of 16 bytes (512 bf16 / 256 fp32 channels): one warp
 // per (row, group), every vector held in registers from its load to its store; a

@@ -156,9 +156,8 @@ __device__ __forceinline__ void split8(const float2* v, uint4& hi, uint4& lo)
     lo = pack8(r);
 }
 
-// v = hi + mid + lo in bf16 each, a pair of them: all of v's 24 bits.  hi is rounded (it
-// stands for v alone in some products); what it leaves has 16 bits, whose upper
-// and lower half are mid and lo.
+// v = hi + mid + lo in bf16 each, a pair of them: all of v's 24 bits.  What the rounded hi
+// leaves has 16 bits, whose upper and lower half are mid and lo.
 __device__ __forceinline__ uint32_t upper2(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
 __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo)
 {
@@ -168,6 +167,7 @@ __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& mid, ui
     const float2 m = unpack2(mid);
     lo = upper2(make_float2(r.x - m.x, r.y - m.y));
 }
+
 // byte offset of 16-byte chunk j of row r in a SW128 tile of 64-element rows
 __device__ __forceinline__ uint32_t chunk_off(int r, int j) { return (uint32_t)(r * 128 + (((j ^ r) & 7) << 4)); }
 template <typename T> __device__ __forceinline__ T& at(void* base, uint32_t off)
@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // there, and dM beyond 2^68 times it no number.  L is formed before anything
             // is scaled, so it is at most 1 wherever dM counts.  (Multiplied in one after the
             // other, the factors took finite rows to NaN; that was 1 % faster, 118.6
-            // us a call of 2048 rows of 128 heads against 120.2.)
+            // us a call of 2048 rows of 128 heads against 120.2 at the time.)
             auto diagonal = [&](int hf, auto factor) {
 #pragma unroll
                 for (int k = 7; k >= 0; --k) {
